@@ -41,12 +41,10 @@ namespace {
 
 // A team of T threads takes a token and holds its row as K octets per thread
 // (octet k T + lane).  K = 0: the row is read twice instead of held.
-DS_HD constexpr int embed_threads(int T) { return T < 128 ? 128 : T; }
-DS_HD constexpr int embed_ctas(int T, int K) { return K <= 4 ? 2048 / embed_threads(T) : 4; } // of an SM
 template <class WT, class YT, int T, int K, int N>
-__global__ void __launch_bounds__(embed_threads(T), embed_ctas(T, K)) k_embed(const __grid_constant__ EParams<N> p)
+__global__ void __launch_bounds__(T < 128 ? 128 : T, K <= 4 ? 2048 / (T < 128 ? 128 : T) : 4) k_embed(const __grid_constant__ EParams<N> p)
 {
-    constexpr int kTeams = embed_threads(T) / T;
+    constexpr int kTeams = (T < 128 ? 128 : T) / T;
     constexpr int KK = K > 0 ? K : 1;
     __shared__ float scratch[kTeams][4 * (T / 32)];
     const int team = threadIdx.x / T, lane = threadIdx.x % T;
@@ -59,11 +57,6 @@ __global__ void __launch_bounds__(embed_threads(T), embed_ctas(T, K)) k_embed(co
     const int64_t id = load_id(sg.ids, sg.ids_i64, t);
     const int nu = sg.nu, cols = sg.cols;
     const bool named = id >= 0 && id < sg.vocab;
-    if (lane == T - 32 && t + p.ahead < p.unit_start[si + 1] - p.unit_start[si]) {
-        const int64_t later = load_id(sg.ids, sg.ids_i64, t + p.ahead);
-        if (later >= 0 && later < sg.vocab)
-            prefetch_l2(static_cast<const WT *>(sg.w) + later * sg.ld, cols * sizeof(WT));
-    }
     const WT *w = static_cast<const WT *>(sg.w) + (named ? id * sg.ld : 0);
     Raw8<WT> row[KK];
     if constexpr (K > 0) {
@@ -1055,16 +1048,14 @@ __global__ void __launch_bounds__(kSumThreads + 64) k_embed_reduce(const __grid_
 }
 
 template <class WT, class YT, int T, int K>
-int launch_rows(EParams<kLmSegs> &p, int64_t units, int sms, cudaStream_t st)
+int launch_rows(const EParams<kLmSegs> &p, int64_t units, cudaStream_t st)
 {
-    constexpr int threads = embed_threads(T);
-    p.ahead = sms * embed_ctas(T, K) * (threads / T) * FRAC;
+    constexpr int threads = T < 128 ? 128 : T;
     const int64_t teams = threads / T, grid64 = (units + teams - 1) / teams;
     const unsigned grid = static_cast<unsigned>(grid64);
     if (p.nseg == 1) {
         EParams<1> one = only_segment(p);
         one.eps = p.eps;
-        one.ahead = p.ahead;
         k_embed<WT, YT, T, K, 1><<<grid, threads, 0, st>>>(one);
     } else {
         k_embed<WT, YT, T, K, kLmSegs><<<grid, threads, 0, st>>>(p);
@@ -1073,17 +1064,17 @@ int launch_rows(EParams<kLmSegs> &p, int64_t units, int sms, cudaStream_t st)
 }
 
 template <class WT, class YT>
-int launch_fwd(EParams<kLmSegs> &p, int cls, int64_t units, int sms, cudaStream_t st)
+int launch_fwd(const EParams<kLmSegs> &p, int cls, int64_t units, cudaStream_t st)
 {
     switch (cls) {
-    case 0: return launch_rows<WT, YT, 32, 1>(p, units, sms, st);
-    case 1: return launch_rows<WT, YT, 32, 2>(p, units, sms, st);
-    case 2: return launch_rows<WT, YT, 128, 1>(p, units, sms, st);
-    case 3: return launch_rows<WT, YT, 128, 2>(p, units, sms, st);
-    case 4: return launch_rows<WT, YT, 256, 2>(p, units, sms, st);
-    case 5: return launch_rows<WT, YT, 256, 4>(p, units, sms, st);
-    case 6: return launch_rows<WT, YT, 256, 8>(p, units, sms, st);
-    default: return launch_rows<WT, YT, 256, 0>(p, units, sms, st);
+    case 0: return launch_rows<WT, YT, 32, 1>(p, units, st);
+    case 1: return launch_rows<WT, YT, 32, 2>(p, units, st);
+    case 2: return launch_rows<WT, YT, 128, 1>(p, units, st);
+    case 3: return launch_rows<WT, YT, 128, 2>(p, units, st);
+    case 4: return launch_rows<WT, YT, 256, 2>(p, units, st);
+    case 5: return launch_rows<WT, YT, 256, 4>(p, units, st);
+    case 6: return launch_rows<WT, YT, 256, 8>(p, units, st);
+    default: return launch_rows<WT, YT, 256, 0>(p, units, st);
     }
 }
 
@@ -1156,12 +1147,12 @@ int embed_class(int64_t cols)
     return 7;
 }
 
-int launch_embed(bool w_bf16, bool y_bf16, int cls, EParams<kLmSegs> &p, int64_t units, int sms, void *stream)
+int launch_embed(bool w_bf16, bool y_bf16, int cls, const EParams<kLmSegs> &p, int64_t units, void *stream)
 {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (w_bf16)
-        return y_bf16 ? launch_fwd<bf16_t, bf16_t>(p, cls, units, sms, st) : launch_fwd<bf16_t, float>(p, cls, units, sms, st);
-    return y_bf16 ? launch_fwd<float, bf16_t>(p, cls, units, sms, st) : launch_fwd<float, float>(p, cls, units, sms, st);
+        return y_bf16 ? launch_fwd<bf16_t, bf16_t>(p, cls, units, st) : launch_fwd<bf16_t, float>(p, cls, units, st);
+    return y_bf16 ? launch_fwd<float, bf16_t>(p, cls, units, st) : launch_fwd<float, float>(p, cls, units, st);
 }
 
 int launch_embed_group(const EGroupParams &p, void *stream)

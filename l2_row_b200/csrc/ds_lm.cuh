@@ -27,13 +27,6 @@ __device__ __forceinline__ void ld32(const void *p, float4 &a, float4 &b)
     a = as_f4(x), b = as_f4(y);
 }
 
-// Asks L2 for `bytes` (below 2^32) from p on, as whole 16 bytes; p 16-byte aligned.
-__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(static_cast<uint32_t>((bytes + 15) / 16 * 16))
-                 : "memory");
-}
-
 // fp32 octets on 32 bytes move in one access: as two of 16 bytes, a warp's
 // accesses would touch every 32-byte sector twice.
 __device__ __forceinline__ bool on32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }

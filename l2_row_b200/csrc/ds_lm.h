@@ -31,7 +31,6 @@ struct EParams {
     int64_t unit_start[N + 1]; // prefix sums of tokens
     int32_t nseg;
     float eps;
-    int32_t ahead; // tokens from a team's row to the row it asks L2 for
 };
 // Their gradient: the rows of the table are dealt to 128 lists by row mod
 // 128, counted in shared memory (kEmbedMaxRows rows a list).
@@ -88,7 +87,7 @@ constexpr int kEmbedZeros = 8192;           // bytes of zeros that bulk copies w
 constexpr int kEmbedSmemMax = 220 * 1024;   // dynamic shared memory of k_embed_reduce
 // Embedding rows (ds_embed.cu): a class by the row length; units: tokens.
 int embed_class(int64_t cols);
-int launch_embed(bool w_bf16, bool y_bf16, int cls, EParams<kLmSegs> &p, int64_t units, int sms, void *stream);
+int launch_embed(bool w_bf16, bool y_bf16, int cls, const EParams<kLmSegs> &p, int64_t units, void *stream);
 int launch_embed_group(const EGroupParams &p, void *stream);
 int launch_embed_reduce(bool w_bf16, bool dy_bf16, int cls, const EGradParams &p, int sms, void *stream);
 

@@ -125,7 +125,7 @@ ds_status run_embed(const ds_eseg *segs, int nseg, ds_dtype w_dtype, ds_dtype ou
             params.unit_start[n] = units;
             params.eps = eps;
             const ds_status st =
-                launched(launch_embed(w_dtype == DS_BF16, out_dtype == DS_BF16, cls, params, units, sm_count(), stream));
+                launched(launch_embed(w_dtype == DS_BF16, out_dtype == DS_BF16, cls, params, units, stream));
             n = 0;
             units = 0;
             return st;
