@@ -8,7 +8,9 @@ there and nowhere else.
 """
 from __future__ import annotations
 
+import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -19,7 +21,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libds.so")
 SOURCES = ["ds_kernels.cu", "ds_tile.cu", "ds_qk.cu", "ds_col.cu", "ds_embed.cu", "ds_qkn.cu", "ds_logp.cu", "ds_api.cpp", "ds_lm_api.cpp"]
-HEADERS = ["ds_internal.h", "ds_host.h", "ds_lm.h", "ds_device.cuh", "ds_lm.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -27,54 +28,93 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-O2,-Wall",
     "-Xptxas", "-warn-spills",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared"]
+LINK_LIBS = ["-lcudart_static", "-lrt", "-lpthread", "-ldl"]
 
 
-def nvcc() -> str:
+def nvcc() -> str | None:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
             return cand
-    raise RuntimeError("nvcc not found: libds.so cannot be built")
+    return None
 
 
-def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    return files + [os.path.join(INCLUDE, "ds.h"), os.path.abspath(__file__)]
+def _digest(*parts) -> str:
+    h = hashlib.sha256()
+    for p in parts:
+        b = p if isinstance(p, bytes) else str(p).encode()
+        h.update(b"%d:" % len(b) + b)
+    return h.hexdigest()
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in _inputs())
+def _read(path: str) -> bytes:
+    with open(path, "rb") as f:
+        return f.read()
 
 
-def _object_is_current(obj: str, dep: str) -> bool:
-    """The object is newer than every project file its last compilation read."""
-    if not (os.path.exists(obj) and os.path.exists(dep)):
-        return False
-    t = os.path.getmtime(obj)
-    with open(dep) as f:
-        read = f.read().split(":", 1)[-1].replace("\\\n", " ").split()
-    own = [p for p in read if os.path.abspath(p).startswith(ROOT)] + [os.path.abspath(__file__)]
-    return all(os.path.exists(p) and os.path.getmtime(p) < t for p in own)
+def _files_of(path: str) -> list[str]:
+    """The source and every header of this project that it includes, at any depth."""
+    todo, found = [path], []
+    while todo:
+        p = todo.pop()
+        if p in found:
+            continue
+        found.append(p)
+        for name in re.findall(rb'^\s*#\s*include\s*"([^"]+)"', _read(p), re.M):
+            for d in (os.path.dirname(p), CSRC, INCLUDE):
+                q = os.path.normpath(os.path.join(d, name.decode()))
+                if os.path.exists(q):
+                    todo.append(q)
+                    break
+    return found
+
+
+def source_key(src: str) -> str:
+    """What an object depends on besides the compiler: the text of its source
+    and headers and the flags.  File times say nothing: a copy does not keep
+    them, and a failed compilation leaves an older object behind."""
+    texts = [(os.path.basename(p), _read(p)) for p in sorted(_files_of(os.path.join(CSRC, src)))]
+    return _digest(" ".join(NVCC_FLAGS), src, *(x for t in texts for x in t))
+
+
+def sources_key() -> str:
+    """What the library depends on besides the compiler."""
+    return _digest(*(source_key(s) for s in SOURCES), " ".join(LINK_FLAGS + LINK_LIBS))
+
+
+def library_keys(lib: str) -> tuple[str, str] | None:
+    """(sources_key, digest of the compiler's version) that a library was built with."""
+    if not os.path.exists(lib):
+        return None
+    m = re.search(rb"libds of sources ([0-9a-f]{64}) by compiler ([0-9a-f]{64})", _read(lib))
+    return (m[1].decode(), m[2].decode()) if m else None
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libds.so if missing or older than its sources; return its path."""
-    if not (force or is_stale()):
+    """Bring libds.so up to date with its sources and the compiler; return its
+    path.  An object's file is named after what it was made of (source_key and
+    the compiler), so one made of anything else is never linked."""
+    cc, have, sources = nvcc(), library_keys(LIB), sources_key()
+    if cc is None:
+        if have and have[0] == sources and not force:
+            return LIB
+        raise RuntimeError("nvcc not found: libds.so cannot be built")
+    version = _digest(subprocess.run([cc, "--version"], capture_output=True, check=True).stdout)
+    keys = (sources, version)
+    if not force and have == keys:
         return LIB
     tmpdir = os.path.join(HERE, "_build")
     os.makedirs(tmpdir, exist_ok=True)
-    objs = []
-    procs = []
+    with open(os.path.join(tmpdir, "key.cpp"), "w") as f:
+        f.write(f'extern "C" const char ds_build_key[] = "libds of sources {keys[0]} by compiler {keys[1]}";\n')
+    objs = [os.path.join(tmpdir, "key.o")]
+    procs = [subprocess.Popen([cc, "-Xcompiler", "-fPIC", "-c", os.path.join(tmpdir, "key.cpp"), "-o", objs[0]])]
     for src in SOURCES:
-        obj = os.path.join(tmpdir, src + ".o")
-        dep = obj + ".d"
+        obj = os.path.join(tmpdir, f"{src}.{_digest(source_key(src), version)[:32]}.o")
         objs.append(obj)
-        if not force and _object_is_current(obj, dep):
+        if not force and os.path.exists(obj):
             continue
-        cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-MMD", "-MF", dep, "-c", os.path.join(CSRC, src),
-               "-o", obj]
+        cmd = [cc, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd))
         procs.append(subprocess.Popen(cmd))
@@ -82,9 +122,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.wait() != 0:
             raise RuntimeError("nvcc failed building libds.so")
     tmp = LIB + ".tmp"
-    subprocess.run([nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs,
-                    "-lcudart_static", "-lrt", "-lpthread", "-ldl"], check=True)
+    subprocess.run([cc, *LINK_FLAGS, "-o", tmp, *objs, *LINK_LIBS], check=True)
     os.replace(tmp, LIB)
+    for name in os.listdir(tmpdir):  # objects of earlier texts
+        if os.path.join(tmpdir, name) not in objs:
+            os.remove(os.path.join(tmpdir, name))
     return LIB
 
 

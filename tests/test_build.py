@@ -1,10 +1,15 @@
-"""Building the library (no GPU): the sources compile, and what is built is
-what the binding loads."""
+"""Building the library (no GPU): the sources compile, what is built is what
+the binding loads, and nothing that was made of other sources takes its place
+(with a compiler that only copies its input)."""
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+
+import pytest
 
 from l2_row_b200 import build
 
@@ -17,3 +22,114 @@ def test_the_sources_build_and_the_binding_loads():
     assert build.build() == build.LIB
     code = "from l2_row_b200 import ds; assert all(hasattr(ds.lib(), n) for n in ds.EXPORTS)"
     subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)
+
+
+# An "object" is its source's text with the headers it names, the "library" all
+# objects; a source that holds BROKEN does not compile.
+COPYING_COMPILER = """#!/bin/sh
+out= src= objs=
+while [ $# -gt 0 ]; do
+    case $1 in
+    --version) echo copying; exit 0;;
+    -o) out=$2; shift;;
+    -c) src=$2; shift;;
+    *.o) objs="$objs $1";;
+    esac
+    shift
+done
+[ -z "$src" ] && exec cat $objs > "$out"
+echo "$src" >> "$LOG"
+echo half > "$out"
+grep -q SLOW "$src" && sleep 1
+grep -q BROKEN "$src" && exit 1
+dir=$(dirname "$src")
+cat "$src" $(sed -n 's/^#include "\\(ds_[a-z_]*\\.cuh\\{0,1\\}\\)"/\\1/p' "$src" | sed "s|^|$dir/|") > "$out"
+[ -z "$LOG" ] || echo "done $src" >> "$LOG"
+"""
+
+
+class Tree:
+    """A copy of the package's sources and build module under `root`."""
+
+    def __init__(self, root):
+        self.root = str(root)
+        spec = importlib.util.spec_from_file_location("tree_build", os.path.join(self.root, "l2_row_b200", "build.py"))
+        self.build = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(self.build)
+
+    @classmethod
+    def copy(cls, root, of=ROOT):
+        for d in ("include", "l2_row_b200"):
+            shutil.copytree(os.path.join(of, d), os.path.join(root, d), copy_function=shutil.copy,
+                            ignore=shutil.ignore_patterns("_build", "*.so", "__pycache__") if of == ROOT else None)
+        return cls(root)
+
+    def path(self, name):
+        return os.path.join(self.root, "l2_row_b200", "csrc", name)
+
+    def edit(self, name, text):
+        with open(self.path(name), "a") as f:
+            f.write(text)
+
+    def library(self):
+        with open(os.path.join(self.root, "l2_row_b200", "libds.so")) as f:
+            return f.read()
+
+    def times(self, when):
+        """Every file of the sources dated `when`."""
+        for d, _, names in os.walk(self.root):
+            for n in names:
+                if "_build" not in d and not n.endswith(".so"):
+                    os.utime(os.path.join(d, n), (when, when))
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    cc = tmp_path / "nvcc"
+    cc.write_text(COPYING_COMPILER)
+    cc.chmod(0o755)
+    monkeypatch.setenv("NVCC", str(cc))
+    monkeypatch.setenv("LOG", str(tmp_path / "log"))
+    t = Tree.copy(str(tmp_path / "tree"))
+    t.build.build()
+    return t
+
+
+def test_objects_of_other_text_are_not_linked(tree, tmp_path):
+    """Whatever the files' times say: sources dated before the objects and the
+    library, a header, a tree copied elsewhere with its objects."""
+    old = os.path.getmtime(os.path.join(tree.root, "l2_row_b200", "libds.so")) - 1000
+    tree.edit("ds_qkn.cu", "\n// first edit\n")
+    tree.times(old)
+    tree.build.build()
+    assert tree.library().count("first edit") == 1
+    tree.edit("ds_lm.cuh", "\n// header edit\n")
+    tree.times(old)
+    tree.build.build()
+    assert tree.library().count("header edit") == 3         # ds_embed.cu, ds_qkn.cu, ds_logp.cu
+    other = Tree.copy(str(tmp_path / "other"), of=tree.root)
+    other.edit("ds_lm.h", "\n// third edit\n")
+    other.edit("ds_logp.cu", "\n// fourth edit\n")
+    other.times(old)
+    other.build.build()
+    lib = other.library()
+    assert lib.count("fourth edit") == 1 and lib.count("first edit") == 1
+    assert "fourth edit" not in tree.library()
+
+
+def test_only_what_changed_is_compiled(tree, tmp_path):
+    log = tmp_path / "log"
+    log.write_text("")
+    assert tree.build.build() and log.read_text() == ""
+    tree.edit("ds_qk.cu", "\n// edit\n")
+    tree.build.build()
+    built = {os.path.basename(x) for x in log.read_text().split("\n") if x and not x.startswith("done")}
+    assert built == {"ds_qk.cu", "key.cpp"}
+
+
+def test_a_current_library_needs_no_compiler(tree, monkeypatch):
+    monkeypatch.setattr(tree.build, "nvcc", lambda: None)
+    assert tree.build.build() == os.path.join(tree.root, "l2_row_b200", "libds.so")
+    tree.edit("ds_qk.cu", "\n// edit\n")
+    with pytest.raises(RuntimeError, match="nvcc not found"):
+        tree.build.build()
