@@ -14,6 +14,7 @@ import re
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -105,28 +106,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmpdir = os.path.join(HERE, "_build")
     os.makedirs(tmpdir, exist_ok=True)
-    with open(os.path.join(tmpdir, "key.cpp"), "w") as f:
-        f.write(f'extern "C" const char ds_build_key[] = "libds of sources {keys[0]} by compiler {keys[1]}";\n')
-    objs = [os.path.join(tmpdir, "key.o")]
-    procs = [subprocess.Popen([cc, "-Xcompiler", "-fPIC", "-c", os.path.join(tmpdir, "key.cpp"), "-o", objs[0]])]
-    for src in SOURCES:
-        obj = os.path.join(tmpdir, f"{src}.{_digest(source_key(src), version)[:32]}.o")
-        objs.append(obj)
-        if not force and os.path.exists(obj):
-            continue
-        cmd = [cc, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd))
-        procs.append(subprocess.Popen(cmd))
-    for p in procs:
-        if p.wait() != 0:
-            raise RuntimeError("nvcc failed building libds.so")
-    tmp = LIB + ".tmp"
-    subprocess.run([cc, *LINK_FLAGS, "-o", tmp, *objs, *LINK_LIBS], check=True)
-    os.replace(tmp, LIB)
+    objs = []
+    # what is being written has a folder of its own: an object or a library
+    # takes its place whole, or, where its compiler failed, not at all
+    with tempfile.TemporaryDirectory(dir=tmpdir) as new:
+        procs = []
+        for src in SOURCES:
+            obj = os.path.join(tmpdir, f"{src}.{_digest(source_key(src), version)[:32]}.o")
+            objs.append(obj)
+            if not force and os.path.exists(obj):
+                continue
+            cmd = [cc, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o",
+                   os.path.join(new, src + ".o")]
+            if verbose:
+                print(" ".join(cmd))
+            procs.append((src, subprocess.Popen(cmd), obj))
+        failed = []
+        for src, p, obj in procs:  # every compiler ends before this call does
+            if p.wait() == 0:
+                os.replace(os.path.join(new, src + ".o"), obj)
+            else:
+                failed.append(src)
+        if failed:
+            raise RuntimeError(f"nvcc failed building libds.so: {', '.join(failed)}")
+        key, lib = os.path.join(new, "key.cpp"), os.path.join(new, "libds.so")
+        with open(key, "w") as f:
+            f.write(f'extern "C" const char ds_build_key[] = "libds of sources {keys[0]} by compiler {keys[1]}";\n')
+        subprocess.run([cc, "-Xcompiler", "-fPIC", "-c", key, "-o", key + ".o"], check=True)
+        subprocess.run([cc, *LINK_FLAGS, "-o", lib, *objs, key + ".o", *LINK_LIBS], check=True)
+        os.replace(lib, LIB)
     for name in os.listdir(tmpdir):  # objects of earlier texts
-        if os.path.join(tmpdir, name) not in objs:
-            os.remove(os.path.join(tmpdir, name))
+        path = os.path.join(tmpdir, name)
+        if os.path.isfile(path) and path not in objs:
+            os.remove(path)
     return LIB
 
 

@@ -124,7 +124,7 @@ def test_only_what_changed_is_compiled(tree, tmp_path):
     tree.edit("ds_qk.cu", "\n// edit\n")
     tree.build.build()
     built = {os.path.basename(x) for x in log.read_text().split("\n") if x and not x.startswith("done")}
-    assert built == {"ds_qk.cu", "key.cpp"}
+    assert built == {"ds_qk.cu", "key.cpp"}        # key.cpp: the library's digest
 
 
 def test_a_current_library_needs_no_compiler(tree, monkeypatch):
@@ -133,3 +133,27 @@ def test_a_current_library_needs_no_compiler(tree, monkeypatch):
     tree.edit("ds_qk.cu", "\n// edit\n")
     with pytest.raises(RuntimeError, match="nvcc not found"):
         tree.build.build()
+
+
+def test_a_failed_build_leaves_everything_as_it_was(tree, tmp_path):
+    """The old library stays, the call ends after every compiler has, no object
+    of a failed compilation is left, and the next build makes what is missing."""
+    before, log = tree.library(), tmp_path / "log"
+    tree.edit("ds_api.cpp", "\nBROKEN\n")
+    tree.edit("ds_tile.cu", "\n// SLOW\n")
+    log.write_text("")
+    with pytest.raises(RuntimeError, match="ds_api.cpp"):
+        tree.build.build()
+    assert tree.library() == before
+    ended = {os.path.basename(x.split()[1]) for x in log.read_text().split("\n") if x.startswith("done")}
+    assert ended == {"ds_tile.cu"}
+    objects = os.path.join(tree.root, "l2_row_b200", "_build")
+    assert sorted(n.split(".")[0] + n[-2:] for n in os.listdir(objects) if n.startswith("ds_api")) == ["ds_api.o"]
+    assert not any(os.path.isdir(os.path.join(objects, n)) for n in os.listdir(objects))
+    with open(tree.path("ds_api.cpp")) as f:
+        text = f.read()
+    with open(tree.path("ds_api.cpp"), "w") as f:
+        f.write(text.replace("BROKEN", "// mended"))
+    tree.build.build()
+    assert tree.library().count("// mended") == 1 and tree.library().count("// SLOW") == 1
+    assert "half" not in tree.library().split("\n")
