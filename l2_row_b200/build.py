@@ -29,7 +29,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-O2,-Wall",
     "-Xptxas", "-warn-spills",
 ]
-LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared"]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xlinker", "-z,defs"]  # no name undefined
 LINK_LIBS = ["-lcudart_static", "-lrt", "-lpthread", "-ldl"]
 
 
@@ -132,7 +132,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         key, lib = os.path.join(new, "key.cpp"), os.path.join(new, "libds.so")
         with open(key, "w") as f:
             f.write(f'extern "C" const char ds_build_key[] = "libds of sources {keys[0]} by compiler {keys[1]}";\n')
-        subprocess.run([cc, "-Xcompiler", "-fPIC", "-c", key, "-o", key + ".o"], check=True)
+        subprocess.run([cc, *NVCC_FLAGS, "-c", key, "-o", key + ".o"], check=True)
         subprocess.run([cc, *LINK_FLAGS, "-o", lib, *objs, key + ".o", *LINK_LIBS], check=True)
         os.replace(lib, LIB)
     for name in os.listdir(tmpdir):  # objects of earlier texts

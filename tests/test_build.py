@@ -157,3 +157,17 @@ def test_a_failed_build_leaves_everything_as_it_was(tree, tmp_path):
     tree.build.build()
     assert tree.library().count("// mended") == 1 and tree.library().count("// SLOW") == 1
     assert "half" not in tree.library().split("\n")
+
+
+@pytest.mark.skipif(build.nvcc() is None, reason="needs nvcc")
+def test_an_undefined_name_is_an_error_of_the_build(tmp_path):
+    """Not of the program that loads the library."""
+    t = Tree.copy(str(tmp_path / "tree"))
+    t.build.SOURCES = ["caller.cpp"]
+    with open(t.path("caller.cpp"), "w") as f:
+        f.write('int not_there(int);\nextern "C" int ds_version(void) { return not_there(1); }\n')
+    with pytest.raises(subprocess.CalledProcessError):
+        t.build.build()
+    assert not os.path.exists(t.build.LIB)
+    t.edit("caller.cpp", "int not_there(int i) { return i; }\n")
+    assert os.path.exists(t.build.build())
