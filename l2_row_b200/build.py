@@ -9,6 +9,7 @@ there and nowhere else.
 from __future__ import annotations
 
 import hashlib
+import mmap
 import os
 import re
 import shutil
@@ -85,10 +86,11 @@ def sources_key() -> str:
 
 def library_keys(lib: str) -> tuple[str, str] | None:
     """(sources_key, digest of the compiler's version) that a library was built with."""
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.getsize(lib):
         return None
-    m = re.search(rb"libds of sources ([0-9a-f]{64}) by compiler ([0-9a-f]{64})", _read(lib))
-    return (m[1].decode(), m[2].decode()) if m else None
+    with open(lib, "rb") as f, mmap.mmap(f.fileno(), 0, access=mmap.ACCESS_READ) as text:
+        m = re.search(rb"libds of sources ([0-9a-f]{64}) by compiler ([0-9a-f]{64})", text)
+        return (m[1].decode(), m[2].decode()) if m else None
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

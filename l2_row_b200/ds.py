@@ -44,11 +44,16 @@ import struct
 from dataclasses import dataclass
 from typing import Any, Sequence
 
+from . import build as _build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libds.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libds.so is not built ({LIB_PATH}); run `python -m l2_row_b200.build`")
+if os.path.isdir(_build.CSRC) and (_build.library_keys(LIB_PATH) or ("",))[0] != _build.sources_key():
+    # its structures and kernels may be others than the ones this module packs arguments for
+    raise ImportError(f"libds.so ({LIB_PATH}) was not built from the sources beside it; run `python -m l2_row_b200.build`")
 
 _lib = ct.CDLL(LIB_PATH)
 

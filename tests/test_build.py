@@ -171,3 +171,18 @@ def test_an_undefined_name_is_an_error_of_the_build(tmp_path):
     assert not os.path.exists(t.build.LIB)
     t.edit("caller.cpp", "int not_there(int i) { return i; }\n")
     assert os.path.exists(t.build.build())
+
+
+def test_the_binding_refuses_a_library_of_other_sources(tmp_path):
+    t = Tree.copy(str(tmp_path / "tree"))
+    os.symlink(build.LIB, t.build.LIB)
+
+    def load():
+        return subprocess.run([sys.executable, "-c", "import l2_row_b200.ds"], cwd=t.root, capture_output=True, text=True)
+
+    assert load().returncode == 0
+    t.edit("ds_lm.h", "\n// another layout\n")
+    r = load()
+    assert r.returncode != 0 and "not built from the sources beside it" in r.stderr
+    shutil.rmtree(os.path.join(t.root, "l2_row_b200", "csrc"))     # a package without sources
+    assert load().returncode == 0
