@@ -580,7 +580,12 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
     }
     __syncthreads();
     const int64_t total = p.unit_start[p.nseg], stride = gridDim.x / CL;
-    bool waiting = true; // a wait that ran out: the rest runs through without, its results do not count
+    // A wait that ran out: the rest runs through without waits, its results do not
+    // count.  A lane that gave up arrives nowhere any more (the lane that arrives for a
+    // warp has waited itself), so the producer reuses a stage only when every consumer
+    // warp has seen it full, no barrier has two copies on their way or an arrival
+    // too many, and whoever depends on that lane runs into its own limit.
+    bool waiting = true;
     auto wait = [&](uint64_t *bar, int phase) {
         if (waiting && !mbar_wait_bounded(bar, phase & 1, p.wait_limit_ns)) {
             raise_device_error(DS_ERR_DEVICE_TIMEOUT, kSiteLogpWait);
@@ -657,7 +662,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
                     a = no_acc();
                 }
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0 && waiting)
                     mbar_arrive(&empty[st]);
                 if (++st == kStages) {
                     st = 0;
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
             }
             part[b][tid] = make_float4(own.m, own.r, own.s, own.w);
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0 && waiting)
                 mbar_arrive(&done[b]);
             if constexpr (CL > 1) {
                 namespace cg = cooperative_groups;
@@ -696,7 +701,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
                 }
                 part[1][tid] = make_float4(own.m, own.r, own.s, own.w);
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0 && waiting)
                     mbar_arrive(&done[1]);
                 return; // one row a cluster
             }
@@ -740,6 +745,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
                                   (h.to - h.from + h.per - 1) / h.per, part[b], gmax[b], sg.top, lane);
         if constexpr (CL > 1) {
             namespace cg = cooperative_groups;
+            __syncwarp(); // (lanes may have left the wait apart)
             cluster_wait();
             if constexpr (TOP)
                 *cg::this_cluster().map_shared_rank(&peer_best[rank * 32 + lane], 0) = key;
@@ -781,7 +787,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
                 t[1] = fmaf(fmaf(d, f.z, f.w), k, t[1]);
         }
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0 && waiting)
             mbar_arrive(&freed[b]);
         warp_sum(t);
         const bool none = M == kNegInf && t[0] == 0.f; // no logit above -inf
