@@ -800,7 +800,9 @@ __global__ void __launch_bounds__(NT + 32 + 32 * kFinishers, kLogpCtas<NT>) k_lo
         };
         if (lane == 0) {
             if (sg.lse)
-                sg.lse[row] = none ? kNegInf : far ? fmaf(M, sg.scale, ln_s) : fmaf(R, kLn2, ln_s);
+                // (the sums stand at R, not at M c: the difference is exact.  R ln 2 would carry
+                // the roundings of c, R and ln 2, each as large as that of the result)
+                sg.lse[row] = none ? kNegInf : fmaf(M, sg.scale, far ? ln_s : fmaf(fmaf(-M, c, R), kLn2, ln_s));
             if (sg.logp)
                 sg.logp[row] = id < 0 ? 0.f : log_prob(xt);
             if (ENT && sg.entropy)
