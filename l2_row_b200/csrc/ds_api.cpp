@@ -82,6 +82,13 @@ static bool side_by_side(const Span &a, const Span &b)
     return d >= a.width && d + b.width <= a.pitch;
 }
 
+// Two matrices of the same bytes whose rows are the same bytes too: other types or
+// pitches can end at the same byte with their rows elsewhere.
+static bool same_rows(const Span &a, const Span &b)
+{
+    return a.width == b.width && (a.pitch == b.pitch || a.hi - a.lo == a.width); // (one row: any pitch)
+}
+
 ds_status check_overlaps(std::vector<Span> &spans)
 {
     std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
@@ -91,7 +98,7 @@ ds_status check_overlaps(std::vector<Span> &spans)
             if (a.role == 0 && b.role == 0)
                 continue;
             const bool exact = a.lo == b.lo && a.hi == b.hi && a.seg == b.seg && a.alias >= 0 &&
-                               a.alias == b.alias;
+                               a.alias == b.alias && same_rows(a, b);
             if (!exact && !side_by_side(a, b))
                 return fail(DS_ERR_OVERLAP, where("an output overlaps another buffer of the call", b.seg));
         }
