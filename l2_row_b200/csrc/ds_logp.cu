@@ -827,6 +827,9 @@ constexpr int kGradThreads = 128;
 
 constexpr int kGradOctets = 2; // octets of a thread, side by side
 
+// exp of it is 0 in fp32, and dh times it finite (for any |dh| below 2^120).
+constexpr float kNoProb = -128.f;
+
 // One octet's gradient: p (A - dh (z - lse)), p = exp(z - lse).  A masked logit
 // (-inf) has p = 0, times a finite value.
 template <bool ENT, class T>
@@ -841,7 +844,7 @@ __device__ __forceinline__ void octet_grad(const Raw8<T> &x, float (&d)[8], floa
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         float2 f = aa;
         if (ENT)
-            f = __ffma2_rn(dd, make_float2(fmaxf(lp.x, -1e30f), fmaxf(lp.y, -1e30f)), aa);
+            f = __ffma2_rn(dd, make_float2(fmaxf(lp.x, kNoProb), fmaxf(lp.y, kNoProb)), aa);
         const float2 o = __fmul2_rn(e, f);
         d[2 * i] = o.x, d[2 * i + 1] = o.y;
     }
