@@ -117,7 +117,8 @@ typedef enum {
     DS_ERR_INVALID_ARG = 1,       /* NULL pointer, bad shape, bad eps, bad dtype value */
     DS_ERR_ALIGNMENT = 2,         /* a row start not 16-byte aligned                    */
     DS_ERR_UNSUPPORTED_DTYPE = 3, /* dtype not allowed for this call                    */
-    DS_ERR_TOO_MANY_SEGMENTS = 4, /* nseg above DS_MAX_SEGMENTS                         */
+    DS_ERR_TOO_MANY_SEGMENTS = 4, /* nseg above DS_MAX_SEGMENTS, or (language-model
+                                     rows) no host memory to check the segments       */
     DS_ERR_CUDA = 5,              /* a CUDA runtime call failed (see ds_last_error)     */
     DS_ERR_DEVICE_TIMEOUT = 6,    /* a bounded device-side wait ran out                 */
     DS_ERR_OVERLAP = 7            /* an output overlaps an input or another output      */

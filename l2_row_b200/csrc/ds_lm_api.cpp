@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <new>
 #include <vector>
 
 #include <cuda_runtime.h>
@@ -884,13 +885,29 @@ ds_status run_logp_grad(const ds_lseg *segs, int nseg, ds_dtype dtype, ds_dtype 
     return flush();
 }
 
+// A call whose checks find no host memory (they list every buffer of the segments,
+// a few MB for DS_MAX_SEGMENTS): an error, as no exception may leave a C function.
+template <class F>
+ds_status guarded(F call)
+{
+    try {
+        return call();
+    } catch (const std::bad_alloc &) {
+        try {
+            return fail(DS_ERR_TOO_MANY_SEGMENTS, "no host memory to check the segments");
+        } catch (const std::bad_alloc &) {
+            return DS_ERR_TOO_MANY_SEGMENTS;
+        }
+    }
+}
+
 } // namespace
 
 extern "C" {
 
 ds_status ds_embed_rows(const ds_eseg *segs, int nseg, ds_dtype w_dtype, ds_dtype out_dtype, float eps, ds_stream stream)
 {
-    return run_embed(segs, nseg, w_dtype, out_dtype, eps, stream);
+    return guarded([&] { return run_embed(segs, nseg, w_dtype, out_dtype, eps, stream); });
 }
 
 uint64_t ds_embed_rows_backward_workspace(int64_t tokens, int64_t vocab, int64_t cols)
@@ -901,12 +918,12 @@ uint64_t ds_embed_rows_backward_workspace(int64_t tokens, int64_t vocab, int64_t
 ds_status ds_embed_rows_backward(const ds_eseg *segs, int nseg, ds_dtype w_dtype, ds_dtype dy_dtype, float eps,
                                  void *workspace, uint64_t workspace_bytes, ds_stream stream)
 {
-    return run_embed_grad(segs, nseg, w_dtype, dy_dtype, eps, workspace, workspace_bytes, stream);
+    return guarded([&] { return run_embed_grad(segs, nseg, w_dtype, dy_dtype, eps, workspace, workspace_bytes, stream); });
 }
 
 ds_status ds_qk_norm_rows(const ds_qnseg *segs, int nseg, ds_dtype dtype, float eps, ds_stream stream)
 {
-    return run_qkn(segs, nseg, dtype, eps, stream);
+    return guarded([&] { return run_qkn(segs, nseg, dtype, eps, stream); });
 }
 
 uint64_t ds_qk_norm_rows_backward_workspace(int64_t head_dim) { return qkn_ws_bytes(head_dim); }
@@ -914,17 +931,17 @@ uint64_t ds_qk_norm_rows_backward_workspace(int64_t head_dim) { return qkn_ws_by
 ds_status ds_qk_norm_rows_backward(const ds_qngseg *segs, int nseg, ds_dtype dtype, ds_dtype grad_dtype, float eps,
                                    float *dwq, float *dwk, void *workspace, uint64_t workspace_bytes, ds_stream stream)
 {
-    return run_qkn_grad(segs, nseg, dtype, grad_dtype, eps, dwq, dwk, workspace, workspace_bytes, stream);
+    return guarded([&] { return run_qkn_grad(segs, nseg, dtype, grad_dtype, eps, dwq, dwk, workspace, workspace_bytes, stream); });
 }
 
 ds_status ds_logp_rows(const ds_lseg *segs, int nseg, ds_dtype dtype, ds_stream stream)
 {
-    return run_logp(segs, nseg, dtype, stream);
+    return guarded([&] { return run_logp(segs, nseg, dtype, stream); });
 }
 
 ds_status ds_logp_rows_backward(const ds_lseg *segs, int nseg, ds_dtype dtype, ds_dtype grad_dtype, ds_stream stream)
 {
-    return run_logp_grad(segs, nseg, dtype, grad_dtype, stream);
+    return guarded([&] { return run_logp_grad(segs, nseg, dtype, grad_dtype, stream); });
 }
 
 } // extern "C"
