@@ -592,7 +592,9 @@ class ESeg:
     def _first(self):
         return self.ids
 
-    def _pack(self, dev=None, w_type=None, y_type=None) -> bytes:
+    def _pack(self, dev=None, w_type=None, y_type=None, call="") -> bytes:
+        """call: "forward" or "backward" packs what that call reads and writes."""
+        fwd, back = call != "backward", call != "forward"
         table = self.w if self.w is not None else self.grad_w
         if table is None:
             raise ValueError("w or grad_w is needed")
@@ -601,18 +603,18 @@ class ESeg:
         f32 = _torch().float32
         ids, wide = _id_vector(self.ids, "ids", T, dev)
         w, ld = _matrix(self.w, "w", V, C, w_type, dev)
-        y, ld_y = _matrix(self.y, "y", T, C, y_type, dev)
-        dy, ld_dy = _matrix(self.dy, "dy", T, C, y_type, dev)
-        gw, ld_g = _matrix(self.grad_w, "grad_w", V, C, f32, dev)
-        if self.y is None:
+        y, ld_y = _matrix(self.y if fwd else None, "y", T, C, y_type, dev)
+        dy, ld_dy = _matrix(self.dy if back else None, "dy", T, C, y_type, dev)
+        gw, ld_g = _matrix(self.grad_w if back else None, "grad_w", V, C, f32, dev)
+        if not y:
             ld_y = ld_dy
-        elif self.dy is not None and ld_y != ld_dy:
+        elif dy and ld_y != ld_dy:
             raise ValueError("y and dy must share a leading dimension")
         one = 1 if self.gain_scalar else 0
         gain = grad_g = 0
         if self.gain is not None:
             gain = _vector(self.gain, "gain", 1 if one else V, f32, dev)
-            grad_g = _vector(self.grad_g, "grad_g", V + one, f32, dev)
+            grad_g = _vector(self.grad_g if back else None, "grad_g", V + one, f32, dev)
         return _ESEG(w, gain, ids, y, dy, gw, grad_g, T, V, C, ld, ld_y, ld_g, self.radius, 1 if self.unit else 0, one,
                      wide, 1 if self.accumulate else 0)
 
@@ -895,7 +897,7 @@ def ds_slerp_rows_backward_noalloc(segs: Sequence, eps: float = 1e-6, dalpha=Non
 
 def ds_embed_rows(segs: Sequence, w_dtype="f32", out_dtype="bf16", eps: float = 1e-6, stream=None) -> None:
     wd, od = _type_code(w_dtype), _type_code(out_dtype)
-    table, n, dev = _packed(segs, ds_eseg, _tensor_type(wd), _tensor_type(od))
+    table, n, dev = _packed(segs, ds_eseg, _tensor_type(wd), _tensor_type(od), "forward")
     _check(_lib.ds_embed_rows(table, n, wd, od, eps, _raw_stream(stream, dev)), "ds_embed_rows")
 
 
@@ -910,7 +912,7 @@ def ds_embed_rows_backward(segs: Sequence, w_dtype="f32", dy_dtype="bf16", eps: 
     ds_embed_rows_backward_workspace(tokens, vocab, cols) of the segments
     (256-byte aligned), or None to have one allocated here for this call."""
     wd, dd = _type_code(w_dtype), _type_code(dy_dtype)
-    table, n, dev = _packed(segs, ds_eseg, _tensor_type(wd), _tensor_type(dd))
+    table, n, dev = _packed(segs, ds_eseg, _tensor_type(wd), _tensor_type(dd), "backward")
     need = 0
     if workspace is None and dev >= 0:
         need = max(ds_embed_rows_backward_workspace(s.tokens, s.vocab, s.cols)
