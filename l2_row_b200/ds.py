@@ -625,6 +625,8 @@ class ESeg:
 def _heads(t, D: int, name: str) -> int:
     if t is None:
         return 0
+    if D < 1:
+        raise ValueError("head_dim must be positive")
     if t.dim() != 2 or t.shape[1] % D:
         raise ValueError(f"{name}: width is not a whole number of heads")
     return t.shape[1] // D

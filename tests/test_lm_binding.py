@@ -26,6 +26,13 @@ def test_a_call_looks_only_at_what_it_reads():
         s.to_c()
 
 
+@pytest.mark.parametrize("seg", [ds.QNSeg, ds.QNGSeg])
+@pytest.mark.parametrize("D", [0, -16])
+def test_head_sizes_below_one(seg, D):
+    with pytest.raises(ValueError, match="head_dim"):
+        seg(D, q=torch.zeros(2, 32)).to_c()
+
+
 @pytest.mark.gpu
 def test_one_segment_for_both_directions():
     T, V, C, g = 40, 50, 96, gen(1)
