@@ -29,7 +29,8 @@ and the language-model rows, each with its gradient:
     ds_logp_rows_backward(segs, dtype, grad_dtype=None, stream=None)
 
 which also check that their tensors have the types the call names and lie on
-the current device (``ValueError``).
+the current device (``ValueError``).  A tensor of one row may have any row
+stride and width.
 
 A segment is a ``WSeg`` / ``ASeg`` of CUDA tensors (2-D, unit column stride,
 row stride = leading dimension) or a raw ``ds_wseg`` / ``ds_aseg`` structure.
@@ -500,7 +501,10 @@ def _matrix(t, name: str, rows: int, cols: int, dtype=None, dev=None) -> tuple[i
         return t.data_ptr(), cols
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: columns must be contiguous")
-    return t.data_ptr(), s0 if rows > 1 else max(s0, cols)
+    if rows > 1:
+        return t.data_ptr(), s0
+    size = t.element_size()  # one row: its stride leads nowhere, and need not be one that the calls take
+    return t.data_ptr(), -(-cols * size // 16) * 16 // size
 
 
 def _vector(t, name: str, n: int, dtype, dev=None) -> int:
