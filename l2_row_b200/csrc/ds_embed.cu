@@ -179,7 +179,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *warp_tot, u
 // kept without barriers: lanes by ballots, warps by a scan of their counts.
 __global__ void __launch_bounds__(kGroupThreads) k_embed_group(const __grid_constant__ EGroupParams p)
 {
-    extern __shared__ __align__(16) unsigned char dyn[];
+    extern __shared__ __align__(128) unsigned char dyn[]; // (every kernel of the file declares it alike)
     int *cnt = reinterpret_cast<int *>(dyn + kGroupSmemFixed); // tokens of each row, then the next place
     __shared__ uint64_t warp_tot[kGroupWarps];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

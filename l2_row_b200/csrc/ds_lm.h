@@ -171,7 +171,7 @@ struct LParams {
 int logp_class(int64_t cols);
 int64_t logp_steps(bool bf16, int64_t cols);
 int launch_logp(bool bf16, int cls, int cl, bool top, bool ent, const LParams<kLmSegs> &p, int64_t units, int sms, void *stream);
-int64_t logp_grad_parts(bool bf16, int64_t cols);
+int64_t logp_grad_parts(int64_t cols); // blocks of a row
 int launch_logp_grad(bool bf16, bool grad_bf16, const LParams<kLmSegs> &p, int64_t units, void *stream);
 
 } // namespace ds

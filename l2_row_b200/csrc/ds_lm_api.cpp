@@ -869,7 +869,7 @@ ds_status run_logp_grad(const ds_lseg *segs, int nseg, ds_dtype dtype, ds_dtype 
     };
     for (int i = 0; i < nseg; ++i) {
         const ds_lseg &s = segs[i];
-        const int64_t parts = logp_grad_parts(dtype == DS_BF16, s.cols);
+        const int64_t parts = logp_grad_parts(s.cols);
         for (int64_t r0 = 0; r0 < s.rows;) {
             if (n == kLmSegs || units + parts > 0x7fffffff)
                 if (ds_status st = flush())

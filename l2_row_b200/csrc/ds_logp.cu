@@ -45,7 +45,7 @@ constexpr int kLogpStages = 4;
 template <int NT>
 constexpr int kLogpCtas = NT == 128 ? 4 : 2; // CTAs of an SM
 constexpr int kCand = 128;  // candidates of the ranking list
-constexpr int kPairs = 128; // groups of threads read again
+constexpr int kAgain = 128; // threads, and groups of threads, that are read again
 constexpr int kFinishers = 3;
 constexpr float kNegInf = -INFINITY;
 constexpr float kFloor = -0x1.92p99f; // bf16 0xF149, about -1e30
@@ -362,8 +362,8 @@ __device__ __forceinline__ float logit(const T *x, int64_t col)
 
 struct TopShared {
     int cols[kCand];
-    int threads[kPairs];
-    int pairs[kPairs]; // group * 1024 + thread
+    int threads[kAgain];
+    int pairs[kAgain]; // group * 1024 + thread
 };
 
 // A logit as the consumers keep the largest of a group: in its own type.
@@ -417,23 +417,23 @@ __device__ __forceinline__ unsigned long long warp_top(TopShared &top, const T *
         for (int w = 0; w < W; ++w) {
             const uint32_t who = __ballot_sync(0xffffffffu, u[w] >= bound);
             const int at = nt + __popc(who & below);
-            if (u[w] >= bound && at < kPairs)
+            if (u[w] >= bound && at < kAgain)
                 top.threads[at] = w * 32 + lane;
             nt += __popc(who);
         }
         __syncwarp();
-        const int items = nt <= kPairs ? nt * OWN : 0;
+        const int items = nt <= kAgain ? nt * OWN : 0;
         for (int i0 = 0; i0 < items; i0 += 32) {
             const int t = top.threads[(i0 + lane) / OWN], g = (i0 + lane) % OWN;
             const bool in = i0 + lane < items && g < groups && widened(gmax[g < groups ? g : 0][t]) >= bound;
             const uint32_t who = __ballot_sync(0xffffffffu, in);
             const int at = np + __popc(who & below);
-            if (in && at < kPairs)
+            if (in && at < kAgain)
                 top.pairs[at] = g * 1024 + t;
             np += __popc(who);
         }
         __syncwarp();
-        if (nt <= kPairs && np <= kPairs) {
+        if (nt <= kAgain && np <= kAgain) {
             // their columns, `per` steps of kUnits units of 16 bytes; eight loads
             // at once, over the pairs or over the steps.  A lane notes its columns
             // in the list at the place that a scan of the lanes' counts gives.
@@ -1024,10 +1024,10 @@ int launch_logp(bool bf16, int cls, int cl, bool top, bool ent, const LParams<kL
     return bf16 ? launch_fwd<bf16_t>(cls, cl, top, ent, p, units, sms, st) : launch_fwd<float>(cls, cl, top, ent, p, units, sms, st);
 }
 
-int64_t logp_grad_parts(bool bf16, int64_t cols)
+int64_t logp_grad_parts(int64_t cols)
 {
-    const int64_t per = int64_t(kGradThreads) * (bf16 ? kGradOctets : kGradOctets);
-    return ((cols + 7) / 8 + per - 1) / per;
+    constexpr int64_t per = 8 * kGradThreads * kGradOctets; // columns of a block
+    return (cols + per - 1) / per;
 }
 
 int launch_logp_grad(bool bf16, bool grad_bf16, const LParams<kLmSegs> &p, int64_t units, void *stream)
