@@ -8,6 +8,7 @@ there and nowhere else.
 """
 from __future__ import annotations
 
+import contextlib
 import hashlib
 import mmap
 import os
@@ -140,7 +141,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for name in os.listdir(tmpdir):  # objects of earlier texts
         path = os.path.join(tmpdir, name)
         if os.path.isfile(path) and path not in objs:
-            os.remove(path)
+            with contextlib.suppress(FileNotFoundError):  # another build's removal
+                os.remove(path)
     return LIB
 
 

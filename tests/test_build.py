@@ -186,3 +186,16 @@ def test_the_binding_refuses_a_library_of_other_sources(tmp_path):
     assert r.returncode != 0 and "not built from the sources beside it" in r.stderr
     shutil.rmtree(os.path.join(t.root, "l2_row_b200", "csrc"))     # a package without sources
     assert load().returncode == 0
+
+
+def test_builds_at_once(tree):
+    """Processes that build one tree together all succeed, on the same library."""
+    tree.edit("ds_tile.cu", "\n// SLOW together\n")
+    code = "from l2_row_b200 import build; build.build()"
+    for edit in range(3):
+        tree.edit("ds_lm.h", f"\n// edit {edit}\n")
+        procs = [subprocess.Popen([sys.executable, "-c", code], cwd=tree.root, stderr=subprocess.PIPE) for _ in range(6)]
+        ends = [(p.communicate()[1], p.returncode) for p in procs]
+        assert all(rc == 0 for _, rc in ends), ends
+        assert tree.build.library_keys(tree.build.LIB)[0] == tree.build.sources_key()
+    assert tree.library().count("SLOW together") == 1
